@@ -589,9 +589,13 @@ def _report(status):
 
 def kvm_rope_table(rope_dims: int, rope_theta: float, n_pos: int, device="cuda", stream=None):
     """(cos, sin) table fp32 [n_pos, rope_dims / 2, 2], built on the device."""
-    out = torch.empty((int(n_pos), int(rope_dims) // 2, 2), dtype=torch.float32, device=device)
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", _device_now())
+    handle = _on_device(device, stream)
+    out = _make(stream, (int(n_pos), int(rope_dims) // 2, 2), torch.float32, device)
     st = lib.kvm_rope_table(int(rope_dims), float(rope_theta), int(n_pos),
-                            out.data_ptr() if out.numel() else None, _on_device(out.device, stream))
+                            out.data_ptr() if out.numel() else None, handle)
     _check(st, None)
     return out
 
