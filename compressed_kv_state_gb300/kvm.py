@@ -643,7 +643,13 @@ class WindowAttention:
 
     def forward(self, q, k, v, out=None, need_lse: bool = False, stream=None):
         """out [B, H, N, 64] (strided like q when not given) of q [B, H, N, 64] and k, v
-        [B, Hkv, N, 64]; with need_lse (out, lse), lse fp32 [B, H, N] for backward()."""
+        [B, Hkv, N, 64]; with need_lse (out, lse), lse fp32 [B, H, N] for backward().
+        autograd does not record the call: tensors that require gradients are refused unless
+        gradients are off (torch.no_grad(), or the forward of a torch.autograd.Function whose
+        backward calls backward())."""
+        if (q.requires_grad or k.requires_grad or v.requires_grad) and torch.is_grad_enabled():
+            raise ValueError("q, k or v requires gradients, and autograd does not record this call: make it under "
+                             "torch.no_grad() (or in a torch.autograd.Function) and take the gradients from backward()")
         dev, dt = q.device, q.dtype
         handle = _on_device(dev, stream)
         rope, kvs, (cfg, at, nbytes, _) = self._plan(q, k)

@@ -24,3 +24,36 @@ def test_rope_table_on_another_stream():
     torch.cuda.synchronize()
     for t in tables:
         assert torch.equal(t, want)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_in_a_function_of_autograd(dt):
+    """forward and backward as a torch.autograd.Function calls them: the gradients that reach the
+    leaves are backward()'s; without the Function the call is refused."""
+    from test_gpu_window import make, op
+    case = (dt, 2, 4, 2, 130, 40, 3, 32, "tokens")
+    q, k, v, dout, rope = make(case, 61)
+    w = op(case, rope)
+
+    class Attend(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, v):
+            out, lse = w.forward(q, k, v, need_lse=True)
+            ctx.save_for_backward(q, k, v, out, lse)
+            return out
+
+        @staticmethod
+        def backward(ctx, dout):
+            q, k, v, out, lse = ctx.saved_tensors
+            return w.backward(q, k, v, out, dout, lse)
+
+    out, lse = w.forward(q, k, v, need_lse=True)
+    want = w.backward(q, k, v, out, dout, lse)
+    leaves = [x.clone().requires_grad_() for x in (q, k, v)]
+    with pytest.raises(ValueError, match="requires gradients"):
+        w.forward(*leaves)
+    got = Attend.apply(*leaves)
+    got.backward(dout)
+    assert torch.equal(got, out)
+    for leaf, x in zip(leaves, want):
+        assert torch.equal(leaf.grad, x)
