@@ -578,6 +578,8 @@ def _make(stream, shape, dtype, device, like=None):
 
 def _report(status):
     """Wait for the device, then report (and clear) a status word as kvm_layer_sync does."""
+    if status is None:
+        raise ValueError("no status word to report from: pass status=torch.zeros(1, dtype=torch.int32, device='cuda')")
     torch.cuda.synchronize(status.device)
     bits = int(status.item())
     if bits:
@@ -627,8 +629,8 @@ class WindowAttention:
     """Sliding-window attention with sink tokens (kvm_window_forward / kvm_window_backward).
 
     window: keys a query sees, itself included; n_sinks: first tokens that stay visible;
-    rope: a kvm_rope_table (None: q and k are not rotated); status: an optional int32 CUDA
-    word for sync()."""
+    rope: a kvm_rope_table (None: q and k are not rotated); status: an int32 CUDA word that
+    the kernels report to, for sync() (None: nothing is reported)."""
 
     def __init__(self, *, window: int, n_sinks: int = 0, rope=None, status=None):
         self.window, self.n_sinks, self.rope, self.status = _held(window), _held(n_sinks), rope, status
@@ -689,9 +691,9 @@ class WindowAttention:
         return dq, dk, dv
 
     def sync(self):
-        """Wait for the device and raise if a kernel reported through the status word."""
-        if self.status is not None:
-            _report(self.status)
+        """Wait for the device and raise if a kernel reported through the status word (which must
+        have been given: without one the kernels' reports are lost)."""
+        _report(self.status)
 
 
 class PagedCache:
@@ -699,7 +701,8 @@ class PagedCache:
 
     k, v: [n_pages, kv_heads, page_size, 64] bf16 or fp32, or uint8 [.., 32] with k_sm, v_sm
     bf16 [n_pages, kv_heads, page_size, 2] (the 4-bit format; dtype is then that of q, k, v
-    and out); rope: a kvm_rope_table, or None; status: an optional int32 CUDA word for sync()."""
+    and out); rope: a kvm_rope_table, or None; status: an int32 CUDA word that the kernels
+    report to, for sync() (None: nothing is reported)."""
 
     def __init__(self, k, v, k_sm=None, v_sm=None, *, dtype=None, rope=None, status=None):
         dev = k.device
@@ -804,6 +807,6 @@ class PagedCache:
         return out
 
     def sync(self):
-        """Wait for the device and raise if a kernel reported through the status word."""
-        if self.status is not None:
-            _report(self.status)
+        """Wait for the device and raise if a kernel reported through the status word (which must
+        have been given: without one the kernels' reports are lost)."""
+        _report(self.status)

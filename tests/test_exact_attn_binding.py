@@ -21,3 +21,9 @@ def test_tensors_that_require_gradients_are_refused(kvm, which):
         w.forward(*x)
     with torch.no_grad(), pytest.raises(ValueError, match="current CUDA device"):  # (the next refusal: a host tensor)
         w.forward(*x)
+
+
+def test_sync_without_a_status_word_is_refused(kvm):
+    """It has nothing to report from, and would pass as if nothing had gone wrong."""
+    with pytest.raises(ValueError, match="status"):
+        kvm.WindowAttention(window=4).sync()

@@ -57,3 +57,11 @@ def test_in_a_function_of_autograd(dt):
     assert torch.equal(got, out)
     for leaf, x in zip(leaves, want):
         assert torch.equal(leaf.grad, x)
+
+
+def test_sync_of_a_cache_without_a_status_word_is_refused():
+    from compressed_kv_state_gb300 import kvm
+    own = kvm.PagedCache.empty(2, 1, 8, dtype=torch.bfloat16)
+    own.sync()
+    with pytest.raises(ValueError, match="status"):
+        kvm.PagedCache(own.k, own.v).sync()
