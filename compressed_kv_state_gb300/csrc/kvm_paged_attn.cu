@@ -258,73 +258,9 @@ __device__ __forceinline__ bool sees(const PagedArgs& a, int p, int j) {
     return j <= p && (a.W == 0 || p - j < a.W || j < a.S);
 }
 
-// dims lane and lane + 32 of a query row, rotated at its position
-template <typename T>
-__device__ __forceinline__ void load_query(const PagedArgs& a, int b, int h, int t, int p, int lane, float (&y)[2]) {
-    const T* q = a.q.at<const T>(b, h, t);
-    const float x0 = to_f<T>(q[lane]), x1 = to_f<T>(q[lane + 32]);
-    const int half = a.r / 2;
-    y[0] = x0;
-    y[1] = x1;
-    if (half == 0 || p < 0) return;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int d = lane + 32 * u, pd = d < half ? d + half : d - half;
-        const float e0 = __shfl_sync(0xffffffffu, x0, pd & 31), e1 = __shfl_sync(0xffffffffu, x1, pd & 31);
-        if (d < a.r) {
-            const float2 cs = a.rope[(int64_t)p * half + (d < half ? d : pd)];
-            const float me = u ? x1 : x0, other = pd < 32 ? e0 : e1;
-            y[u] = d < half ? me * cs.x - other * cs.y : me * cs.x + other * cs.y;
-        }
-    }
-}
-
-// One query row from the keys that it sees alone, by one warp, one key at a time: for rows
-// whose products met a value that is not finite in a key of another query's.
-template <typename T, bool I4> __device__ __noinline__ void row_alone(const PagedArgs& a, int b, int h, int t, int lane) {
-    Span s;
-    s.of(a, b, false);
-    const int p = s.oldest + t;
-    float q[2], m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
-    load_query<T>(a, b, h, t, p, lane, q);
-    if (sizeof(T) == 2) {
-        q[0] = __bfloat162float(__float2bfloat16_rn(q[0]));
-        q[1] = __bfloat162float(__float2bfloat16_rn(q[1]));
-    }
-    auto cached = [&](const void* pages, const uint32_t* sm, int64_t row, float& x0, float& x1) {
-        if constexpr (!I4) {
-            const T* r = reinterpret_cast<const T*>(pages) + row * D;
-            x0 = to_f<T>(r[lane]);
-            x1 = to_f<T>(r[lane + 32]);
-        } else {
-            const uint8_t* r = reinterpret_cast<const uint8_t*>(pages) + row * (D / 2) + (lane >> 1);
-            const uint32_t w = sm[row];
-            const int sh = (lane & 1) * 4;
-            x0 = fmaf(lo_f(w), (float)((r[0] >> sh) & 15), hi_f(w));
-            x1 = fmaf(lo_f(w), (float)((r[16] >> sh) & 15), hi_f(w));
-        }
-    };
-    for (int step = 0; step < s.steps; ++step)
-        for (int j = s.base(step); j < s.base(step) + KS && j <= p; ++j) {
-            if (!sees(a, p, j)) continue;
-            const int64_t row = paged_row(a, b, h / a.G, j);
-            if (row < 0) continue;
-            float k0, k1, v0, v1;
-            cached(a.k, a.k_sm, row, k0, k1);
-            cached(a.v, a.v_sm, row, v0, v1);
-            const float x = warp_sum(q[0] * k0 + q[1] * k1) * a.scale_log2;
-            const bool nan = !(x == x);
-            const float mn = nan ? x : fmaxf(m, x);
-            const float al = mn == m ? 1.f : ex2(m - mn), e = nan ? x : x == mn ? 1.f : ex2(x - mn);
-            m = mn;
-            l = l * al + e;
-            o0 = o0 * al + e * v0;
-            o1 = o1 * al + e * v1;
-        }
-    const float il = l == 0.f ? 0.f : 1.f / l;
-    T* out = a.out.at<T>(b, h, t);
-    out[lane] = from_f<T>(o0 * il);
-    out[lane + 32] = from_f<T>(o1 * il);
+// some half of a word of two bf16, or a word that is an fp32 value, is not finite
+template <typename T> __device__ __forceinline__ bool odd_word(uint32_t w) {
+    return (w & 0x7f800000u) == 0x7f800000u || (sizeof(T) == 2 && (w & 0x7f80u) == 0x7f80u);
 }
 
 template <int F, int MT>
@@ -648,9 +584,31 @@ __global__ void __launch_bounds__(Cfg<F, MT>::THREADS, 1)
         // keep: keys that some query sees and whose page exists; whole: every row sees every key
         uint32_t keep = good[ring_id * C::STAGES + st];
         bool whole = oldest >= base + KS - 1 && (a.W == 0 || cp.s.len - 1 - base < a.W || base + KS <= a.S);
+        // alone: keys that some queries see and others do not (the newest of a.T tokens, and with a
+        // window the first) whose value is not finite.  A product would carry it to the others, as
+        // 0 x NaN is NaN: their values are left out of it and reach the rows that see them apart.
+        uint32_t alone = 0;
         if (!whole || keep != ap.all_runs) {
             whole = false;
-            keep = __ballot_sync(0xffffffffu, ((keep >> (lane >> ap.run_bits)) & 1) && wanted(cp.s, base + lane));
+            const int j = base + lane;
+            const bool in = ((keep >> (lane >> ap.run_bits)) & 1) && wanted(cp.s, j);
+            keep = __ballot_sync(0xffffffffu, in);
+            if (a.T > 1) {
+                const bool part = in && !(j <= oldest && (a.W == 0 || cp.s.len - 1 - j < a.W || j < a.S));
+                if (__any_sync(0xffffffffu, part)) {
+                    bool odd = false;
+                    if constexpr (C::I4) {
+                        odd = odd_word<__nv_bfloat16>(*reinterpret_cast<const uint32_t*>(sk + C::SMO + (KS + lane) * 4));
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < C::RB / 16; ++x) {
+                            const uint4 y = *reinterpret_cast<const uint4*>(sv + (x >> 3) * KS * 128 + lane * 128 + (((x & 7) ^ (lane & 7)) << 4));
+                            odd = odd || odd_word<T>(y.x) || odd_word<T>(y.y) || odd_word<T>(y.z) || odd_word<T>(y.w);
+                        }
+                    }
+                    alone = __ballot_sync(0xffffffffu, part && odd);
+                }
+            }
         } else {
             keep = ~0u;
         }
@@ -689,8 +647,16 @@ __global__ void __launch_bounds__(Cfg<F, MT>::THREADS, 1)
             }
             if (!whole) {  // scales of keys that are not there may be anything
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (!((keep >> (8 * j + tg)) & 1)) ksm[j] = vsm[j] = 0;
+                for (int j = 0; j < 4; ++j) {
+                    const int k = 8 * j + tg;
+                    if (!((keep >> k) & 1)) ksm[j] = vsm[j] = 0;
+                    if (alone >> k & 1) {  // (scale or least value is not finite: no dim of the row is)
+                        vsm[j] = 0;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (sees(a, pos[e], base + k)) vmin[0][e] = NAN;
+                    }
+                }
             }
             // (scale, least value and offset as below, two queries at once)
             float2 s2[4];
@@ -823,8 +789,16 @@ __global__ void __launch_bounds__(Cfg<F, MT>::THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (!((keep >> (8 * j + (e ? kb : ka))) & 1)) ksm[j][e] = vsm[j][e] = 0;
+                        for (int e = 0; e < 2; ++e) {
+                            const int k = 8 * j + (e ? kb : ka);
+                            if (!((keep >> k) & 1)) ksm[j][e] = vsm[j][e] = 0;
+                            if (alone >> k & 1) {  // (scale or least value is not finite: no dim of the row is)
+                                vsm[j][e] = 0;
+#pragma unroll
+                                for (int r = 0; r < 2 * MT; ++r)
+                                    if (sees(a, pos[r], base + k)) vmin[r >> 1][r & 1] = NAN;
+                            }
+                        }
                 }
             }
             // scale and least value of a key's row enter its score, the codes' offset of 128 leaves:
@@ -928,7 +902,7 @@ __global__ void __launch_bounds__(Cfg<F, MT>::THREADS, 1)
                             vf[x][2 * w + 1] = __byte_perm(av[w], bv[w], 0x7632);
                         }
                         if (!whole) {  // 0 x NaN is NaN: rows that are not there become zeros
-                            const uint32_t z = (((keep >> ta) & 1) ? 0xffffu : 0u) | (((keep >> tb) & 1) ? 0xffff0000u : 0u);
+                            const uint32_t in = keep & ~alone, z = (((in >> ta) & 1) ? 0xffffu : 0u) | (((in >> tb) & 1) ? 0xffff0000u : 0u);
 #pragma unroll
                             for (int w = 0; w < 8; ++w) vf[x][w] &= z;
                         }
@@ -948,6 +922,41 @@ __global__ void __launch_bounds__(Cfg<F, MT>::THREADS, 1)
                     const uint32_t pa[4] = {P[mt][2 * i][0], P[mt][2 * i][1], P[mt][2 * i + 1][0], P[mt][2 * i + 1][1]};
 #pragma unroll
                     for (int nt = 0; nt < 8; ++nt) mma16816(O[mt][nt], pa, vf[0][nt], vf[1][nt]);
+                }
+            }
+            if constexpr (!C::I4) {
+                if (alone) {  // rare
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll 1
+                        for (uint32_t left = (alone >> (8 * j)) & 0xff; left; left &= left - 1) {
+                            // the key's column of P is with lane `from` of the row's four, dims 16 c .. with this one
+                            const int x = __ffs(left) - 1, k = 8 * j + x, from = (lane & ~3) | (x < 4 ? x : (x + 2) & 3);
+                            float p[MT][2];
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
+                                    const uint32_t w = __shfl_sync(0xffffffffu, P[mt][j][u], from);
+                                    p[mt][u] = x < 4 ? lo_f(w) : hi_f(w);
+                                }
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const uint4 y = *reinterpret_cast<const uint4*>(sv + 128 * k + (((2 * c + e) ^ (k & 7)) << 4));
+                                const uint32_t v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                                    for (int u = 0; u < 2; ++u) {
+                                        if (!sees(a, pos[2 * mt + u], base + k)) continue;
+#pragma unroll
+                                        for (int z = 0; z < 4; ++z) {
+                                            O[mt][2 * z][2 * u + e] = fmaf(p[mt][u], lo_f(v[z]), O[mt][2 * z][2 * u + e]);
+                                            O[mt][2 * z + 1][2 * u + e] = fmaf(p[mt][u], hi_f(v[z]), O[mt][2 * z + 1][2 * u + e]);
+                                        }
+                                    }
+                            }
+                        }
                 }
             }
         } else {
@@ -991,19 +1000,23 @@ __global__ void __launch_bounds__(Cfg<F, MT>::THREADS, 1)
             }
             __syncwarp();
             // two dims a lane for the sum, four keys at once
+            auto value = [&](int t) {
+                if constexpr (!C::I4) {
+                    return *reinterpret_cast<const float2*>(sv + (lane >> 4) * KS * 128 + t * 128 + ((((lane >> 1) & 7) ^ (t & 7)) << 4) + (lane & 1) * 8);
+                } else {
+                    const uint32_t sm = *reinterpret_cast<const uint32_t*>(sk + C::SMO + KS * 4 + t * 4);
+                    const uint32_t u = sv[t * 32 + lane];
+                    return make_float2(fmaf(lo_f(sm), (float)(u & 15), hi_f(sm)), fmaf(lo_f(sm), (float)(u >> 4), hi_f(sm)));
+                }
+            };
+            const uint32_t with = keep & ~alone;
 #pragma unroll 2
             for (int t = 0; t < KS; t += 4) {
                 float2 v[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    if constexpr (!C::I4) {
-                        v[x] = *reinterpret_cast<const float2*>(sv + (lane >> 4) * KS * 128 + (t + x) * 128 + ((((lane >> 1) & 7) ^ ((t + x) & 7)) << 4) + (lane & 1) * 8);
-                    } else {
-                        const uint32_t sm = *reinterpret_cast<const uint32_t*>(sk + C::SMO + KS * 4 + (t + x) * 4);
-                        const uint32_t u = sv[(t + x) * 32 + lane];
-                        v[x] = make_float2(fmaf(lo_f(sm), (float)(u & 15), hi_f(sm)), fmaf(lo_f(sm), (float)(u >> 4), hi_f(sm)));
-                    }
-                    if (!((keep >> (t + x)) & 1)) v[x] = make_float2(0.f, 0.f);  // (0 x NaN is NaN)
+                    v[x] = value(t + x);
+                    if (!((with >> (t + x)) & 1)) v[x] = make_float2(0.f, 0.f);  // (0 x NaN is NaN)
                 }
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
@@ -1018,6 +1031,19 @@ __global__ void __launch_bounds__(Cfg<F, MT>::THREADS, 1)
                     acc[r][1] = y.y;
                 }
             }
+#pragma unroll 1
+            for (uint32_t left = alone; left; left &= left - 1) {  // rare
+                const int t = __ffs(left) - 1;
+                const float2 v = value(t);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    if (r >= nr) break;
+                    if (!sees(a, oldest + r0 + r - ap.by_t.div(r0 + r) * a.T, base + t)) continue;
+                    const float w = pw[r * KS + t];
+                    acc[r][0] = fmaf(w, v.x, acc[r][0]);
+                    acc[r][1] = fmaf(w, v.y, acc[r][1]);
+                }
+            }
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(empty(ring_id, st));  // the stage may be filled again
@@ -1028,7 +1054,6 @@ __global__ void __launch_bounds__(Cfg<F, MT>::THREADS, 1)
         if (last || at + 1 == count) {
             const bool direct = last && at - seg + 1 == cp.s.steps;
             float* const part = a.part + (size_t)(2 * gw + (seg == 0 ? 0 : 1)) * ap.pl.slot;
-            bool odd = false;  // some row of this lane is not finite
             if constexpr (C::SWAP) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -1047,10 +1072,6 @@ __global__ void __launch_bounds__(Cfg<F, MT>::THREADS, 1)
                     if (direct) {
                         const int gt = r0 + r;
                         __nv_bfloat16* o = a.out.at<__nv_bfloat16>(cp.b, hk * a.G + gt / a.T, gt % a.T) + 8 * g;
-                        float z = 0.f;
-#pragma unroll
-                        for (int w = 0; w < 8; ++w) z = fmaf(y[w], 0.f, z);
-                        odd |= !(z == 0.f) || !(ls == ls);
                         *reinterpret_cast<uint4*>(o) = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
                     } else {
                         float* o = part + (size_t)r * (D + 2);
@@ -1082,10 +1103,6 @@ __global__ void __launch_bounds__(Cfg<F, MT>::THREADS, 1)
                         if (direct) {
                             const int gt = r0 + r;
                             __nv_bfloat16* o = a.out.at<__nv_bfloat16>(cp.b, hk * a.G + gt / a.T, gt % a.T) + 16 * c;
-                            float z = 0.f;
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) z = fmaf(y[x], 0.f, z);
-                            odd |= !(z == 0.f) || !(ls == ls);
 #pragma unroll
                             for (int x = 0; x < 2; ++x)
                                 reinterpret_cast<uint4*>(o)[x] =
@@ -1107,20 +1124,14 @@ __global__ void __launch_bounds__(Cfg<F, MT>::THREADS, 1)
                         const float mul = ls > 0.f ? 1.f / ls : 0.f;
                         const int gt = r0 + r;
                         float* o = a.out.at<float>(cp.b, hk * a.G + gt / a.T, gt % a.T) + 2 * lane;
-                        const float y0 = acc[r][0] * mul, y1 = acc[r][1] * mul;
-                        odd |= !(fmaf(y0, 0.f, y1 * 0.f) == 0.f) || !(ls == ls);
-                        o[0] = y0;
-                        o[1] = y1;
+                        o[0] = acc[r][0] * mul;
+                        o[1] = acc[r][1] * mul;
                     } else {
                         float* o = part + (size_t)r * (D + 2);
                         *reinterpret_cast<float2*>(o + 2 * lane) = make_float2(acc[r][0], acc[r][1]);
                         if (lane == 0) *reinterpret_cast<float2*>(o + D) = make_float2(m[r], ls);
                     }
                 }
-            }
-            if (a.T > 1 && __any_sync(0xffffffffu, odd)) {
-                __syncwarp();
-                for (int r = 0; r < nr; ++r) row_alone<T, C::I4>(a, cp.b, hk * a.G + (r0 + r) / a.T, (r0 + r) % a.T, lane);
             }
             fresh = true;
         }
@@ -1133,7 +1144,7 @@ __global__ void __launch_bounds__(Cfg<F, MT>::THREADS, 1)
 // are added up in turn.  Sixteen warps where items are few and so have many parts, one
 // where they are many (a block then takes sixteen rows).
 constexpr int JT = 512;
-template <typename T, bool I4, int JW> __global__ void __launch_bounds__(JT) paged_join_kernel(const __grid_constant__ AttnP ap) {
+template <typename T, int JW> __global__ void __launch_bounds__(JT) paged_join_kernel(const __grid_constant__ AttnP ap) {
     __shared__ float sums[JT / 32][D + 2];
     const PagedArgs& a = ap.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, jw = JW == 1 ? 0 : warp;
@@ -1198,15 +1209,9 @@ template <typename T, bool I4, int JW> __global__ void __launch_bounds__(JT) pag
         }
     }
     const float il = l > 0.f ? 1.f / l : 0.f;
-    o0 *= il;
-    o1 *= il;
     T* out = a.out.at<T>(b, h, t) + 2 * lane;
-    out[0] = from_f<T>(o0);
-    out[1] = from_f<T>(o1);
-    if (a.T > 1 && __any_sync(0xffffffffu, !(fmaf(o0, 0.f, o1 * 0.f) == 0.f) || !(l == l))) {
-        __syncwarp();
-        row_alone<T, I4>(a, b, h, t, lane);
-    }
+    out[0] = from_f<T>(o0 * il);
+    out[1] = from_f<T>(o1 * il);
 }
 
 size_t first_bytes(const PagedArgs& a) { return ((size_t)(a.B + 1) * 4 + 255) / 256 * 256; }
@@ -1252,8 +1257,8 @@ template <int F, int MT> cudaError_t run(const PagedArgs& a, cudaStream_t s) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return many ? cudaLaunchKernelEx(&cfg, paged_join_kernel<typename C::T, C::I4, 1>, p)
-                : cudaLaunchKernelEx(&cfg, paged_join_kernel<typename C::T, C::I4, JT / 32>, p);
+    return many ? cudaLaunchKernelEx(&cfg, paged_join_kernel<typename C::T, 1>, p)
+                : cudaLaunchKernelEx(&cfg, paged_join_kernel<typename C::T, JT / 32>, p);
 }
 
 // f<format, m-tiles>() for the call's format and row count: 32 rows at once from 17 on, and in 4

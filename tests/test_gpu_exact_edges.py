@@ -65,3 +65,78 @@ def test_sync_of_a_cache_without_a_status_word_is_refused():
     own.sync()
     with pytest.raises(ValueError, match="status"):
         kvm.PagedCache(own.k, own.v).sync()
+
+
+def fastest(f):
+    """The least of three calls' times on the device, in milliseconds (after one not counted)."""
+    ms = []
+    for _ in range(4):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        b.record()
+        b.synchronize()
+        ms.append(a.elapsed_time(b))
+    return min(ms[1:])
+
+
+@pytest.mark.parametrize("dt,int4", [("bf16", False), ("bf16", True), ("fp32", False), ("fp32", True)])
+def test_a_value_that_every_query_sees_costs_the_paged_attention_nothing(dt, int4):
+    """A first value that is not finite makes every result so; the call takes its usual time (rows
+    computed again key by key took 500 times that; 10 leaves room for the clock)."""
+    from test_gpu_paged import filled
+    cache, _, q, lens, table, _ = filled((dt, int4, 1, 2, 1, 2, 40000, 16, 0, 0, 32), 3)
+    clean = fastest(lambda: cache.attend(q, lens, table))
+    one = torch.ones(1, 1, 1, 64, dtype=q.dtype, device="cuda")
+    cache.append(one, one * float("nan"), lens * 0, table)
+    assert torch.isnan(cache.attend(q, lens, table)).all()
+    assert fastest(lambda: cache.attend(q, lens, table)) <= 10 * clean
+
+
+@pytest.mark.parametrize("case", [
+    ("bf16", False, 3, 4, 4, 5, 700, 16, 0, 0, 32), ("bf16", False, 2, 8, 2, 7, 333, 8, 0, 0, 16),
+    ("bf16", False, 2, 24, 1, 3, 900, 64, 100, 16, 0), ("bf16", False, 3, 4, 2, 16, 400, 32, 40, 3, 32),
+    ("bf16", False, 2, 2, 2, 4, 20, 8, 2, 0, 0), ("fp32", False, 3, 4, 4, 5, 700, 16, 0, 0, 32),
+    ("fp32", False, 2, 24, 1, 3, 900, 64, 100, 16, 0), ("fp32", False, 2, 2, 2, 4, 20, 8, 2, 0, 0)],
+    ids=lambda c: "-".join(map(str, c)))
+def test_dims_of_keys_that_some_queries_see(case):
+    """Values of the newest tokens, and with a window of the first that any query sees, are not
+    finite in some dims: those dims of the queries that see them are not either, every other
+    result is as near its definition as without them."""
+    from exact_attn_testlib import visible, within
+    from test_gpu_paged import filled, reference
+    dtype, int4, B, H, Hkv, T, max_len, page, W, S, r = case
+    cache, held, q, lens, table, rope = filled(case, 71)
+    ref, bound = reference(case, held, q, lens, rope)
+    hit = torch.zeros(q.shape, dtype=torch.bool, device="cuda")
+    for b in range(B):
+        n = int(lens[b])
+        i = n - T + torch.arange(T, device="cuda")
+        first = max(0, n - T - W + 1) if W else 0
+        marks = [(n - 1, 5, float("inf")), (n - 2, 17, float("nan")), (n - 2, 40, -float("inf")), (n - T + 1, 63, float("nan")),
+                 (first, 0, float("inf")), (first + 1, 33, float("nan"))]
+        for j, d, x in marks:
+            if not max(0, n - T - W + 1 if W else n - T + 1) <= j < n:
+                continue
+            cache.v[int(table[b, j // page]), :, j % page, d] = x
+            hit[b, :, visible(i, torch.tensor([j], device="cuda"), W, S)[:, 0], d] = True
+    out = cache.attend(q, lens, table, window=W, n_sinks=S)
+    cache.sync()
+    assert hit.any() and not torch.isfinite(out[hit]).any()
+    zero = torch.zeros((), device="cuda")
+    within(torch.where(hit, zero.to(out.dtype), out), torch.where(hit, zero.double(), ref), bound, "the others")
+
+
+@pytest.mark.parametrize("dt,int4", [("bf16", False), ("bf16", True), ("fp32", False), ("fp32", True)])
+def test_queries_before_the_first_token_beside_values_that_are_not_finite(dt, int4):
+    """A sequence shorter than its queries, all of its values NaN: the queries that see nothing
+    get zeros, the others NaN."""
+    from test_gpu_paged import filled
+    for H in (2, 6, 10):  # rows of a key head: 8, 24, 40
+        case = (dt, int4, 1, H, 1, 4, 2, 8, 0, 0, 32)
+        cache, _, q, lens, table, _ = filled(case, 72)
+        one = torch.ones(1, 1, 2, 64, dtype=q.dtype, device="cuda")
+        cache.append(one, one * float("nan"), lens * 0, table)
+        out = cache.attend(q, lens, table)
+        cache.sync()
+        assert torch.equal(out[:, :, :2], torch.zeros_like(out[:, :, :2])) and torch.isnan(out[:, :, 2:]).all()
