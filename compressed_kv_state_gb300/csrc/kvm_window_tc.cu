@@ -24,8 +24,7 @@
 // queries here, in warps of their own, slowed the softmax by more than the pass takes.
 //
 // A product with P reads whole blocks, and 0 x NaN is NaN: a row whose result is not
-// finite is computed again by its thread from the keys that it sees alone, so values
-// behind the mask never reach it.
+// finite is looked at again (repair_rows), so values behind the mask never reach it.
 //
 // All mbarrier waits are bounded (about two seconds); on expiry the CTA raises the
 // status word, lets its copies and MMAs land, and exits.
@@ -53,6 +52,7 @@ constexpr int TMEM_COLS = 512, TMEM_SLOT = 256;  // of a slot: S (128), O (64), 
 constexpr int NTHREADS = 384;
 // launched with 168 registers a thread (64512): 128 x 64 + 256 x 216 = 63488
 constexpr int REGS_LOW = 64, REGS_HIGH = 216;
+constexpr float LOWEST = -3.4028234663852886e38f;
 constexpr float TAU = 8.0f;  // lazy-rescale threshold (log2 units)
 
 enum {
@@ -118,39 +118,127 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
     }
 }
 
-// One query row from the keys it sees alone (fp32 softmax of the same bf16 operands):
-// for rows whose block products met a value that is not finite.  Slow, and rare: only
-// rows within a block of such a value come here.  The result goes to the row of the
-// output tile in shared memory.
-__device__ __noinline__ void row_alone(const TcArgs& a, int b, int h, int hk, int64_t p, uint8_t* row, int sw) {
-    float q[D], o[D];
-    const __nv_bfloat16* qp = a.q.at<const __nv_bfloat16>(b, h, p);
-    const __nv_bfloat16* qq = a.split ? a.q_in.at<const __nv_bfloat16>(b, h, p) : qp;
-    for (int x = 0; x < D; ++x) {
-        q[x] = __bfloat162float(x < 32 ? qp[x] : qq[x]);
-        o[x] = 0.f;
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ bool odd(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+
+// s[y] of a lane becomes its own and lane ^ W's s[y] or, in the upper of the two, s[y + W]
+template <int W> __device__ __forceinline__ void halve(float (&s)[32], int lane) {
+#pragma unroll
+    for (int y = 0; y < W; ++y) {
+        const float give = lane & W ? s[y] : s[y + W], have = lane & W ? s[y + W] : s[y];
+        s[y] = have + __shfl_xor_sync(0xffffffffu, give, W);
     }
-    float m = -INFINITY, l = 0.f;
-    const int64_t ws = p - a.W + 1 > 0 ? p - a.W + 1 : 0, sinks = a.S < ws ? a.S : ws;
-    for (int64_t n = 0; n < sinks + p + 1 - ws; ++n) {
-        const int64_t j = n < sinks ? n : ws + n - sinks;
-        const __nv_bfloat16* kp = a.k.at<const __nv_bfloat16>(b, hk, j);
-        const __nv_bfloat16* kq = a.split ? a.k_in.at<const __nv_bfloat16>(b, hk, j) : kp;
-        const __nv_bfloat16* vp = a.v.at<const __nv_bfloat16>(b, hk, j);
-        float s = 0.f;
-        for (int x = 0; x < D; ++x) s = fmaf(q[x], __bfloat162float(x < 32 ? kp[x] : kq[x]), s);
-        s *= a.scale_log2;
-        const bool nan = !(s == s);
-        const float mn = nan ? s : fmaxf(m, s);
-        const float al = mn == m ? 1.f : ex2(m - mn), e = nan ? s : s == mn ? 1.f : ex2(s - mn);
-        m = mn;
-        l = l * al + e;
-        for (int x = 0; x < D; ++x) o[x] = o[x] * al + e * __bfloat162float(vp[x]);
-        if (nan) break;  // a score that is no number: neither is the row
+}
+
+// Rows of a warp whose results are not finite, by the whole warp: bit r of `rows` is query p0 + r,
+// whose maximum and sum of weights are lane r's m and l, whose result is row r at `out`.
+//
+// Such a result is right where a key that the row sees is to blame.  But a product multiplies
+// whole blocks and 0 x NaN is NaN, so it may also be a value of a key in the tile's blocks that
+// the row does not see.  Those are few, at most 127 before the window of the warp's last row and
+// 254 behind its first, and are looked at first.  Dims that such a value reaches are computed
+// again from the keys that the row does see, until none of them can become finite any more; at
+// most 381 rows of a head come this far for one such value.  Four rows and eight keys at a time,
+// two dims a lane: 1,700 cycles (a NaN in every head of B1 H2 N16384, causal: 190 us where every
+// later row sees it, 7.6 ms where 127 rows of a tile do not).  Meanwhile `work` is counted up, so
+// that the CTA's waits last.
+__device__ __noinline__ void repair_rows(const TcArgs& a, const Tile& T, int p0, uint32_t rows, float m, float l, uint8_t* out,
+                                         volatile int* work) {
+    constexpr uint32_t ALL = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    auto below = [](int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; };
+    auto word = [&](const Rows& x, int h, int j, int w) { return reinterpret_cast<const uint32_t*>(x.at<const __nv_bfloat16>(T.b, h, j))[w]; };
+    const Rows &qr = a.split && lane >= 16 ? a.q_in : a.q, &kr = a.split && lane >= 16 ? a.k_in : a.k;
+    // bit r: dim 2 lane (bad0) or 2 lane + 1 (bad1) of row r is reached by a key out of its sight
+    uint32_t bad0 = 0, bad1 = 0;
+    auto look = [&](int j, int end) {
+#pragma unroll 8
+        for (; j < end; ++j) {
+            const uint32_t w = word(a.v, T.hk, j, lane), blind = below(j - p0) | (j >= a.S ? ~below(j + a.W - p0) : 0);
+            if (odd(lo_f(w))) bad0 |= blind;
+            if (odd(hi_f(w))) bad1 |= blind;
+        }
+    };
+    const int end = min(T.ws + KB * (T.nblk - T.sink), a.N);
+    if (T.sink) look(p0 + 1, a.S);  // (rows past the sinks' are zeros in their block)
+    look(T.ws, min(p0 + 32 - a.W, min(p0 + 1, end)));
+    look(max(p0 + 1, T.ws), end);
+    rows &= __reduce_or_sync(ALL, bad0 | bad1);
+    __syncwarp();  // (each row has been stored by its own lane)
+    while (rows) {
+        int r[4], p[4];  // (p -1: no row)
+        float q0[4], q1[4], o0[4], o1[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            r[x] = rows ? __ffs(rows) - 1 : 0;
+            p[x] = rows ? p0 + r[x] : -1;
+            rows &= rows - 1;
+            const uint32_t w = p[x] >= 0 ? word(qr, T.h, p[x], lane) : 0;
+            q0[x] = lo_f(w);
+            q1[x] = hi_f(w);
+            o0[x] = o1[x] = 0.f;
+        }
+        const int px = p[0] < 0 ? -1 : lane < 8 ? p[0] : lane < 16 ? p[1] : lane < 24 ? p[2] : p[3];  // of this lane's score
+        const float mx = __shfl_sync(ALL, m, lane < 8 ? r[0] : lane < 16 ? r[1] : lane < 24 ? r[2] : r[3]);
+        const int last = max(max(p[0], p[1]), max(p[2], p[3])), ws = max(p[0] - a.W + 1, 0), sinks = min(a.S, ws);
+        const int chunks = (sinks + 7) / 8, n = chunks + (last - ws) / 8 + 1;  // of eight keys: sinks, then from ws on
+        uint32_t kw[8], vw[8];
+        auto fetch = [&](int i) {
+            const int j0 = i < chunks ? 8 * i : ws + 8 * (i - chunks);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int j = min(j0 + u, a.N - 1);
+                kw[u] = word(kr, T.hk, j, lane);
+                vw[u] = word(a.v, T.hk, j, lane);
+            }
+        };
+        fetch(0);
+        for (int i = 0; i < n; ++i) {
+            float s[32];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) s[8 * x + u] = fmaf(q1[x], hi_f(kw[u]), q0[x] * lo_f(kw[u]));
+            uint32_t v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = vw[u];
+            if (i + 1 < n) fetch(i + 1);
+            // lane 8 x + u ends with the sum of row x and key u over the lanes
+            halve<16>(s, lane);
+            halve<8>(s, lane);
+            halve<4>(s, lane);
+            halve<2>(s, lane);
+            halve<1>(s, lane);
+            const int j = (i < chunks ? 8 * i : ws + 8 * (i - chunks)) + (lane & 7);
+            const bool seen = (i >= chunks || j < sinks) && j <= px && (px - j < a.W || j < a.S);
+            const float e = seen ? ex2(fmaf(s[0], a.scale_log2, -mx)) : -0.f;  // (a weight is never -0)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float w = __shfl_sync(ALL, e, 8 * x + u);
+                    const bool skip = __float_as_uint(w) == 0x80000000u;
+                    o0[x] = skip ? o0[x] : fmaf(w, lo_f(v[u]), o0[x]);
+                    o1[x] = skip ? o1[x] : fmaf(w, hi_f(v[u]), o1[x]);
+                }
+            if ((i & 63) == 63) {
+                bool may = false;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    may = may || (p[x] >= 0 && (((bad0 >> r[x] & 1) && !odd(o0[x])) || ((bad1 >> r[x] & 1) && !odd(o1[x]))));
+                if (!__any_sync(ALL, may)) break;
+                if (lane == 0) *work = *work + 1;
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float il = 1.f / __shfl_sync(ALL, l, r[x]);
+            __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(out + r[x] * 128 + ((((lane >> 2) ^ (r[x] & 7)) << 4) | ((lane & 3) << 2)));
+            if (p[x] >= 0 && (bad0 >> r[x] & 1)) y[0] = __float2bfloat16_rn(o0[x] * il);
+            if (p[x] >= 0 && (bad1 >> r[x] & 1)) y[1] = __float2bfloat16_rn(o1[x] * il);
+        }
     }
-    for (int x = 0; x < D; ++x)
-        *reinterpret_cast<__nv_bfloat16*>(row + ((((x >> 3) ^ sw) << 4) | ((x & 7) << 1))) = __float2bfloat16_rn(o[x] / l);
-    if (a.lse) a.lse[((int64_t)b * a.H + h) * a.N + p] = m + log2f(l);
 }
 
 __global__ void __launch_bounds__(NTHREADS, 1)
@@ -165,6 +253,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NSLOT * NBAR);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* work = abort_flag + 1;  // (counted up by repair_rows)
     auto bar = [&](int slot, int i) { return smem_u32(bars + slot * NBAR + i); };
     // turn k of slot s is tile blockIdx.x + (NSLOT k + s) * gridDim.x
     auto tile_id = [&](int slot, int k) -> int {
@@ -190,6 +279,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             mbar_init(bar(s, B_FINAL), 1);
         }
         *abort_flag = 0;
+        *work = 0;
         fence_barrier_init();
         fence_proxy_async();
     }
@@ -215,7 +305,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 const int id = tile_id(slot, k);
                 if (id < 0) break;
                 const Tile T = tile_of(a, id);
-                if (k >= 1 && !mbar_wait_idle(bar(slot, B_QEMPTY), (k - 1) & 1, abort_flag, a.status)) break;
+                if (k >= 1 && !mbar_wait_idle(bar(slot, B_QEMPTY), (k - 1) & 1, abort_flag, a.status, work)) break;
                 {
                     const uint32_t dq = sbase + OFF_Q + slot * Q_BYTES, full = bar(slot, B_QFULL);
                     mbar_expect_tx(full, Q_BYTES);
@@ -230,13 +320,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     const bool sink = j < T.sink;
                     const int key0 = sink ? KB * j : T.ws + KB * (j - T.sink);
                     const uint32_t bytes = sink ? (uint32_t)a.SW * 128 : (uint32_t)KV_BYTES;
-                    if (g >= NS && !mbar_wait_idle(bar(slot, B_KEMPTY + st), (g / NS - 1) & 1, abort_flag, a.status)) { ok = false; break; }
+                    if (g >= NS && !mbar_wait_idle(bar(slot, B_KEMPTY + st), (g / NS - 1) & 1, abort_flag, a.status, work)) { ok = false; break; }
                     mbar_expect_tx(bar(slot, B_KFULL + st), bytes);
                     tma_load_4d(dk, sink ? &tm_sk : &tm_k, 0, key0, T.hk, T.b, bar(slot, B_KFULL + st));
                     if (a.split)
                         tma_load_4d(dk + KV_BYTES / 2, sink ? &tm_skh : &tm_kh, 32, key0, T.hk, T.b, bar(slot, B_KFULL + st));
                     last_k = g;
-                    if (g >= NS && !mbar_wait_idle(bar(slot, B_VEMPTY + st), (g / NS - 1) & 1, abort_flag, a.status)) { ok = false; break; }
+                    if (g >= NS && !mbar_wait_idle(bar(slot, B_VEMPTY + st), (g / NS - 1) & 1, abort_flag, a.status, work)) { ok = false; break; }
                     mbar_expect_tx(bar(slot, B_VFULL + st), bytes);
                     tma_load_4d(dv, sink ? &tm_sv : &tm_v, 0, key0, T.hk, T.b, bar(slot, B_VFULL + st));
                     last_v = g;
@@ -273,8 +363,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // S = Q K^T of block gb, once the softmax has read block gb - 1's S
             auto issue_qk = [&](int gb, bool sink, bool last) -> bool {
                 const int st = gb % NS;
-                if (gb > 0 && !mbar_wait_warp_idle(bar(slot, B_SFREE), (gb - 1) & 1, abort_flag, a.status)) return false;
-                if (!mbar_wait_warp_idle(bar(slot, B_KFULL + st), (gb / NS) & 1, abort_flag, a.status)) return false;
+                if (gb > 0 && !mbar_wait_warp_idle(bar(slot, B_SFREE), (gb - 1) & 1, abort_flag, a.status, work)) return false;
+                if (!mbar_wait_warp_idle(bar(slot, B_KFULL + st), (gb / NS) & 1, abort_flag, a.status, work)) return false;
                 tc_fence_after();
                 const uint64_t dk = dk0 + (uint64_t)(st * (KV_BYTES >> 4));
                 if (lead) {
@@ -293,14 +383,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 const int id = tile_id(slot, k);
                 if (id < 0) break;
                 const Tile T = tile_of(a, id);
-                if (!mbar_wait_warp_idle(bar(slot, B_QFULL), k & 1, abort_flag, a.status)) break;
+                if (!mbar_wait_warp_idle(bar(slot, B_QFULL), k & 1, abort_flag, a.status, work)) break;
                 tc_fence_after();
                 if (!issue_qk(g, T.sink > 0, T.nblk == 1)) break;
                 for (int j = 0; j < T.nblk; ++j) {
                     const int gj = g + j, st = gj % NS;
                     if (j + 1 < T.nblk && !issue_qk(gj + 1, j + 1 < T.sink, j + 2 == T.nblk)) { ok = false; break; }
-                    if (!mbar_wait_warp_idle(bar(slot, B_PFULL), gj & 1, abort_flag, a.status) ||
-                        !mbar_wait_warp_idle(bar(slot, B_VFULL + st), (gj / NS) & 1, abort_flag, a.status)) {
+                    if (!mbar_wait_warp_idle(bar(slot, B_PFULL), gj & 1, abort_flag, a.status, work) ||
+                        !mbar_wait_warp_idle(bar(slot, B_VFULL + st), (gj / NS) & 1, abort_flag, a.status, work)) {
                         ok = false;
                         break;
                     }
@@ -338,7 +428,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (id < 0) break;
             const Tile T = tile_of(a, id);
             const int p = T.q0 + row;
-            float m_used = -INFINITY, l = 0.0f;
+            float m_used = LOWEST, l = 0.0f;  // (finite: scores of -infinity before any other get weights of 0)
             for (int j = 0; j < T.nblk; ++j) {
                 const int gj = g + j;
                 const bool sink = j < T.sink;
@@ -352,7 +442,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 const int lo_min = cap(w0 - off) * !sink, lo_max = cap(w0 + 31 - off) * !sink;
                 const int groups = sink ? (a.SW + 31) / 32 : KB / 32;  // of 32 columns
                 constexpr uint32_t ALL = (1u << (KB / 32)) - 1;
-                if (!mbar_wait_warp_idle(bar(slot, B_SFULL), gj & 1, abort_flag, a.status)) { ok = false; break; }
+                if (!mbar_wait_warp_idle(bar(slot, B_SFULL), gj & 1, abort_flag, a.status, work)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t v[KB / 32][32];
 #pragma unroll
@@ -396,7 +486,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 bool rescale = false;
                 float alpha = 1.0f;
                 if (mblk > m_used) {
-                    if (m_used == -INFINITY) {
+                    if (m_used == LOWEST) {
                         m_used = mblk;
                     } else if (mblk > m_used + TAU) {
                         alpha = ex2(m_used - mblk);
@@ -406,7 +496,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 }
                 l *= alpha;
                 // the previous block's PV has read P and updated O
-                if (gj > 0 && !mbar_wait_warp_idle(bar(slot, B_PVDONE), (gj - 1) & 1, abort_flag, a.status)) { ok = false; break; }
+                if (gj > 0 && !mbar_wait_warp_idle(bar(slot, B_PVDONE), (gj - 1) & 1, abort_flag, a.status, work)) { ok = false; break; }
                 tc_fence_after();
                 // tensor-memory loads and stores are warp-wide: the whole warp rescales when any
                 // of its rows must (the others by 1)
@@ -469,7 +559,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // epilogue: O / l (a query sees itself: l > 0) through the last block's K stage
             const int gl = g + T.nblk - 1, st = gl % NS;
             uint8_t* const tile = smem + OFF_K + (slot * NS + st) * KV_BYTES;
-            if (!mbar_wait_warp_idle(bar(slot, B_PVDONE), gl & 1, abort_flag, a.status)) { ok = false; break; }
+            if (!mbar_wait_warp_idle(bar(slot, B_PVDONE), gl & 1, abort_flag, a.status, work)) { ok = false; break; }
             tc_fence_after();
             const float il = 1.0f / l;
             const float2 il2 = make_float2(il, il);
@@ -494,11 +584,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             tc_fence_before();
             if (a.lse && p < a.N) a.lse[((int64_t)T.b * a.H + T.h) * a.N + p] = m_used + log2f(l);
-            if (!(sum.x + sum.y == 0.f) && p < a.N) row_alone(a, T.b, T.h, T.hk, p, tile + row * 128, row & 7);
+            // (without a sum above 0 a score is no number, or all are -infinity: nor is any dim then)
+            const uint32_t strange = __ballot_sync(0xffffffffu, !(sum.x + sum.y == 0.f) && p < a.N && l > 0.f);
+            if (strange) repair_rows(a, T, T.q0 + (row & ~31), strange, m_used, l, tile + (row & ~31) * 128, work);
             fence_proxy_async();
             mbar_arrive(bar(slot, B_OUT));
             if (row == 0) {
-                ok = mbar_wait_idle(bar(slot, B_OUT), k & 1, abort_flag, a.status);
+                ok = mbar_wait_idle(bar(slot, B_OUT), k & 1, abort_flag, a.status, work);
                 if (ok) tma_store_4d(&tm_o, smem_u32(tile), 0, T.q0, T.h, T.b);
                 bulk_commit();
                 held = st;
@@ -664,7 +756,8 @@ cudaError_t launch_win_fwd_tc(const WinArgs& a, void* scratch, cudaStream_t s) {
     msv = mv;
     if (ok && a.S > 0)
         ok = make_tmap_bf16_4d(&msk, t.k.p, N, Hkv, B, t.k.sn, t.k.sh, t.k.sb, sw, 4, half_row, half_row) &&
-             make_tmap_bf16_4d(&msv, t.v.p, N, Hkv, B, t.v.sn, t.v.sh, t.v.sb, sw);
+             // (ends with the sinks: the block's further rows are zeros, whatever those keys' values are)
+             make_tmap_bf16_4d(&msv, t.v.p, (uint64_t)a.S, Hkv, B, t.v.sn, t.v.sh, t.v.sb, sw);
     if (ok && t.split)
         ok = make_tmap_bf16_4d(&mqh, a.q.p, N, (uint64_t)a.H, B, a.q.sn, a.q.sh, a.q.sb, 128, 4, 64, 32) &&
              make_tmap_bf16_4d(&mkh, a.k.p, N, Hkv, B, a.k.sn, a.k.sh, a.k.sb, KB, 4, 64, 32) &&

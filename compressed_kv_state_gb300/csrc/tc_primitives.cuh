@@ -81,10 +81,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 // The same wait with the thread suspended between looks (up to 10 us each) instead of
-// polling: for roles that wait most of the time beside warps that compute.
-__device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+// polling: for roles that wait most of the time beside warps that compute.  work (optional): a
+// word of the CTA that rare, long but finite work counts up; the limit starts anew while it moves.
+__device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                               volatile int* work = nullptr) {
     if (mbar_try(bar, parity)) return true;
-    const long long t0 = clock64();
+    long long t0 = clock64();
+    int seen = 0;
     for (;;) {
         uint32_t ok;
         asm volatile(
@@ -97,6 +100,11 @@ __device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, vo
         if (ok) return true;
         if (*abort_flag) return false;
         if (clock64() - t0 > (1ll << 32)) {
+            if (work && *work != seen) {
+                seen = *work;
+                t0 = clock64();
+                continue;
+            }
             *abort_flag = 1;
             if (status) atomicOr(status, STATUS_TIMEOUT);
             return false;
@@ -109,8 +117,9 @@ __device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, vo
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
 }
-__device__ __forceinline__ bool mbar_wait_warp_idle(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
-    return __all_sync(0xffffffffu, mbar_wait_idle(bar, parity, abort_flag, status));
+__device__ __forceinline__ bool mbar_wait_warp_idle(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                                    volatile int* work = nullptr) {
+    return __all_sync(0xffffffffu, mbar_wait_idle(bar, parity, abort_flag, status, work));
 }
 
 __device__ __forceinline__ void fence_barrier_init() {

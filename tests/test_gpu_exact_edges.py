@@ -140,3 +140,81 @@ def test_queries_before_the_first_token_beside_values_that_are_not_finite(dt, in
         out = cache.attend(q, lens, table)
         cache.sync()
         assert torch.equal(out[:, :, :2], torch.zeros_like(out[:, :, :2])) and torch.isnan(out[:, :, 2:]).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("where", [0, 130, 5000])
+def test_a_value_that_later_queries_see_costs_the_window_nothing(dt, where):
+    """Under the causal mask a value that is not finite makes every later result so; the call takes
+    about its usual time (rows computed again key by key took 150 times that)."""
+    from compressed_kv_state_gb300 import kvm
+    g = torch.Generator().manual_seed(81)
+    n = 16384 if dt == "bf16" else 6000
+    q, k, v = (torch.randn(1, 2, n, 64, generator=g).to(torch.bfloat16 if dt == "bf16" else torch.float32).cuda() for _ in range(3))
+    w = kvm.WindowAttention(window=n)
+    clean = w.forward(q, k, v)
+    usual = fastest(lambda: w.forward(q, k, v))
+    for x in (float("nan"), float("inf")):
+        v[:, :, where] = x
+        out = w.forward(q, k, v)
+        assert not torch.isfinite(out[:, :, where:]).any()
+        assert torch.equal(out[:, :, :where // 128 * 128 - 128], clean[:, :, :where // 128 * 128 - 128]) or where < 256
+        assert fastest(lambda: w.forward(q, k, v)) <= 10 * usual
+
+
+# dtype, B, H, Hkv, N, W, S, r, layout
+DIMS = [
+    ("bf16", 1, 4, 2, 700, 100, 4, 32, "heads"), ("bf16", 2, 2, 2, 1000, 130, 20, 0, "tokens"),
+    ("bf16", 1, 2, 1, 640, 640, 0, 64, "heads"), ("bf16", 1, 2, 1, 300, 7, 128, 16, "heads"),
+    ("bf16", 1, 24, 8, 2000, 256, 3, 32, "tokens"), ("fp32", 1, 4, 2, 700, 100, 4, 32, "heads"),
+    ("fp32", 1, 2, 1, 300, 7, 128, 16, "heads"),
+]
+
+
+@pytest.mark.parametrize("case", DIMS, ids=["-".join(map(str, c)) for c in DIMS])
+def test_dims_of_values_that_some_queries_see(case):
+    """Values that are not finite in some dims, a key of the sinks and the keys next to them among
+    them: those dims of the queries that see them are not finite either, every other result is as
+    near its definition as without them."""
+    from exact_attn_testlib import visible, window64, within
+    from test_gpu_window import make, op
+    dt, B, H, Hkv, N, W, S, r, layout = case
+    q, k, v, _, rope = make(case, 82)
+    ref, bound = window64(q, k, v, W, S, rope, q.dtype)
+    hit = torch.zeros(q.shape, dtype=torch.bool, device="cuda")
+    i = torch.arange(N, device="cuda")
+    inf, nan = float("inf"), float("nan")
+    marks = [(S, 1, nan), (S + 1, 2, inf), (N // 3, 5, inf), (N // 3 + 1, 5, -inf), (N // 2, 17, nan), (N // 2 + 40, 63, -inf), (N - 1, 9, nan)]
+    if S:
+        marks.append((S - 1, 0, inf))
+    for j, d, x in marks:
+        v[:, :, j, d] = x
+        hit[:, :, visible(i, torch.tensor([j], device="cuda"), W, S)[:, 0], d] = True
+    w = op(case, rope, torch.zeros(1, dtype=torch.int32, device="cuda"))
+    out = w.forward(q, k, v)
+    w.sync()
+    assert not torch.isfinite(out[hit]).any()
+    zero = torch.zeros((), device="cuda")
+    within(torch.where(hit, zero.to(out.dtype), out), torch.where(hit, zero.double(), ref), bound, "the others")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_scores_of_minus_infinity(dt):
+    """Keys that are -infinity under queries of ones: a query that sees one key more than those is the
+    mean of the rest, one that sees only those has no softmax (NaN by the definition)."""
+    from compressed_kv_state_gb300 import kvm
+    dtype = torch.bfloat16 if dt == "bf16" else torch.float32
+    g = torch.Generator().manual_seed(83)
+    q = torch.ones(1, 1, 300, 64, dtype=dtype, device="cuda")
+    k, v = q.clone(), torch.randn(1, 1, 300, 64, generator=g).to(dtype).cuda()
+    k[:, :, :140] = -float("inf")
+    out, lse = kvm.WindowAttention(window=300).forward(q, k, v, need_lse=True)
+    assert torch.isnan(out[:, :, :140]).all()
+    rest = v[0, 0, 140:].double()
+    n = torch.arange(1, 161, device="cuda")[:, None]
+    ref = rest.cumsum(0) / n
+    # equal weights of 1: the sum's and the result's rounding
+    u = 2.0 ** -8 if dt == "bf16" else 2.0 ** -24
+    assert ((out[0, 0, 140:].double() - ref).abs() <= u * ref.abs() + 240 * 2.0 ** -23 * rest.abs().cumsum(0) / n).all()
+    score = 8.0 * 1.4426950408889634  # 64 / 8 in log2 units
+    assert ((lse[0, 0, 140:].double() - (score + n[:, 0].double().log2())).abs() <= 1e-4).all()
