@@ -94,8 +94,9 @@ __device__ __forceinline__ void add2(float (&a)[4], float p, const float4& v) {
     const float2 hi = __ffma2_rn(make_float2(p, p), make_float2(v.z, v.w), make_float2(a[2], a[3]));
     a[0] = lo.x, a[1] = lo.y, a[2] = hi.x, a[3] = hi.y;
 }
-// acc[i][0..3] += sum_k P[ty + 16 i][k] * V[k][4 tx ..]; skip: a zero weight hides its row of V
-// (a masked key's value may be anything)
+// acc[i][0..3] += sum_k P[ty + 16 i][k] * V[k][4 tx ..]; skip: a weight of -0 hides its row of V
+// (a masked key's value may be anything; a key that is seen has a weight of +0 at least, and one
+// too small for fp32 does not hide that its value is not finite)
 template <bool SKIP>
 __device__ __forceinline__ void mm_nn(float (&acc)[4][4], const float* P, const float* V, int ty, int tx) {
 #pragma unroll 2
@@ -109,7 +110,7 @@ __device__ __forceinline__ void mm_nn(float (&acc)[4][4], const float* P, const 
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float w = x == 0 ? p[i].x : x == 1 ? p[i].y : x == 2 ? p[i].z : p[i].w;
-                if (SKIP && w == 0.f) continue;
+                if (SKIP && __float_as_uint(w) == 0x80000000u) continue;
                 add2(acc[i], w, v);
             }
         }
@@ -216,10 +217,11 @@ __global__ void __launch_bounds__(NT, 2) win_fwd_kernel(const WinArgs a) {
         for (int i = 0; i < 4; ++i) {
             const int64_t qi = q0 + ty + 16 * i;
             float mx = -INFINITY;
+            bool seen[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int64_t kj = k0 + tx + 16 * j;
-                const bool ok = kj < k1 && visible(qi, kj, a.W, a.S);
+                const bool ok = seen[j] = kj < k1 && visible(qi, kj, a.W, a.S);
                 full = full && ok;
                 c[i][j] = ok ? c[i][j] * a.scale_log2 : -INFINITY;
                 mx = fmaxf(mx, c[i][j]);
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(NT, 2) win_fwd_kernel(const WinArgs a) {
             for (int j = 0; j < 4; ++j) {
                 const float p = exp2f(c[i][j] - mz);
                 sum += p;
-                sp[(ty + 16 * i) * LD + tx + 16 * j] = p;
+                sp[(ty + 16 * i) * LD + tx + 16 * j] = seen[j] ? p : -0.f;
             }
 #pragma unroll
             for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);

@@ -218,3 +218,23 @@ def test_scores_of_minus_infinity(dt):
     assert ((out[0, 0, 140:].double() - ref).abs() <= u * ref.abs() + 240 * 2.0 ** -23 * rest.abs().cumsum(0) / n).all()
     score = 8.0 * 1.4426950408889634  # 64 / 8 in log2 units
     assert ((lse[0, 0, 140:].double() - (score + n[:, 0].double().log2())).abs() <= 1e-4).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_a_value_under_a_weight_that_underflows(dt):
+    """A score 2,500 below the others: the key's weight is not zero by the definition, so a value
+    there that is not finite reaches every query that sees it, also in a tile with masked keys."""
+    from compressed_kv_state_gb300 import kvm
+    dtype = torch.bfloat16 if dt == "bf16" else torch.float32
+    q = torch.zeros(1, 1, 200, 64, dtype=dtype, device="cuda")
+    k, v = torch.zeros_like(q), torch.ones_like(q)
+    q[..., 0] = 100.0
+    k[:, :, 0, 0], v[:, :, 0, 3] = -200.0, float("nan")
+    for w in (kvm.WindowAttention(window=200), kvm.WindowAttention(window=50, n_sinks=1), kvm.WindowAttention(window=7)):
+        out = w.forward(q, k, v)
+        seen = min(200, w.window) if not w.n_sinks else 200
+        assert torch.isnan(out[:, :, :seen, 3]).all()
+        rest = torch.cat([out[:, :, :seen, :3].flatten(), out[:, :, seen:].flatten()])
+        # weights of exactly 1, so the sums are whole numbers n; 1 / n is off by 2^-24 of itself at most,
+        # n times that is rounded once more: 2^-24 + 2^-24, and their product 2^-48, off 1 (bf16: to 1)
+        assert ((rest.double() - 1.0).abs() <= 2.0 ** -23 + 2.0 ** -48).all()
