@@ -365,7 +365,7 @@ namespace kv {
 constexpr int OFF_K = 0, OFF_V = TILE, OFF_Q = 2 * TILE, OFF_DO = OFF_Q + NS * BLK, OFF_LD = OFF_DO + NS * BLK;
 constexpr int OFF_BAR = OFF_LD + NS * 512, SMEM = OFF_BAR + 256 + 1024;
 constexpr int T_S = 0, T_DP = 64, T_DV = 128, T_DK = 192;  // P^T over S^T, dS^T over dP^T
-enum { B_KV = 0, B_FULL, B_EMPTY = B_FULL + NS, B_SPD = B_EMPTY + NS, B_P = B_SPD + 2, B_DONE = B_P + 2, B_OUT, NBAR };
+enum { B_KV = 0, B_FULL, B_EMPTY = B_FULL + NS, B_SPD = B_EMPTY + NS, B_P = B_SPD + 2, B_READ = B_P + 2, B_DONE = B_READ + 2, B_OUT, NBAR };
 
 __global__ void __launch_bounds__(NTHREADS, 2)
     win_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
@@ -438,13 +438,15 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         const uint64_t dq0 = sdesc_sw128(sbase + OFF_Q, 16, 1024), ddo0 = sdesc_sw128(sbase + OFF_DO, 16, 1024);
         const uint64_t mq0 = sdesc_sw128(sbase + OFF_Q, BLK, 1024), mdo0 = sdesc_sw128(sbase + OFF_DO, BLK, 1024);
         bool ok = mbar_wait_warp(bar(B_KV), 0, abort_flag, a.status);
-        // by halves of 32 queries, the warpgroups' in turn: half s's S^T and dP^T go out (in issue
-        // order after half s - 2's products, which read P^T and dS^T there), then half s - 1's
-        // dV and dK once its rows are done
+        // by halves of 32 queries, the warpgroups' in turn: half s's S^T and dP^T go out once half
+        // s - 2's products have read P^T and dS^T there (the tensor core keeps the order of
+        // products only where they share shape and accumulator), then half s - 1's dV and dK once
+        // its rows are done
         for (int s = 0; ok && s <= 2 * n; ++s) {
             if (s < 2 * n) {
                 const int j = s >> 1, st = j % NS, hf = s & 1;
                 if (!hf && !mbar_wait_warp(bar(B_FULL + st), (j / NS) & 1, abort_flag, a.status)) break;
+                if (j > 0 && !mbar_wait_warp(bar(B_READ + hf), (j - 1) & 1, abort_flag, a.status)) break;
                 tc_fence_after();
                 const uint64_t off = st * (BLK >> 4) + hf * (32 * 128 >> 4);
                 const uint32_t tS = tmem + T_S + 32 * hf, tD = tmem + T_DP + 32 * hf;
@@ -468,6 +470,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
                     for (int ks = 0; ks < 2; ++ks) mma_bf16_ts(tmem + T_DV, tS + 8 * ks, mdo0 + off + 128 * ks, id_o, (s > 1 || ks > 0) ? 1u : 0u);
 #pragma unroll
                     for (int ks = 0; ks < 2; ++ks) mma_bf16_ts(tmem + T_DK, tD + 8 * ks, mq0 + off + 128 * ks, id_o, (s > 1 || ks > 0) ? 1u : 0u);
+                    mma_commit(bar(B_READ + hf));
                     if (hf) mma_commit(bar(B_EMPTY + st));
                 }
                 __syncwarp();
