@@ -15,7 +15,12 @@
 // only wait, multiply and release.  With the loads in the computing warps themselves a
 // step cost them about as long again.  An item inside one warp's part is written at once;
 // parts of an item split over warps go to scratch and are joined by a second kernel in
-// the order of the warps, so results do not depend on timing.
+// the order of the warps, so results do not depend on timing.  The grid is this card's 152
+// SMs whatever part of them a call gets, as the scratch's size and the sums' order follow it.
+//
+// Queries of one sequence see nearly the same keys.  The few that only some of them see are
+// looked at when they come by; where their value is not finite, it stays out of the products
+// and is added row by row (four queries a sequence: 1 to 2% of a call, 6% of 64 short windows).
 //
 // bf16 pages: mma.sync m16n8k16 with fp32 sums, K and V fragments by 16-byte shared
 // loads (dims and tokens are permuted alike on both sides of each product, which lets a
@@ -31,8 +36,8 @@
 // through movmatrix): half the products, and no exponentials for rows that are not there
 // (57.5 to 51.2 us for the same sequences; the rest is unpacking, which does not shrink).
 // fp32: the same walk with fp32 multiply-adds, a lane a key for the scores and two dims
-// a lane for the sum: 152 us for 24 sequences to 16,000 keys, 16 heads of 4 (3.9 TB/s), 5.7
-// TB/s with a row a key head.  Bound by those with more rows; latencies count, so eight warps
+// a lane for the sum: 152 us for 24 sequences to 16,000 keys, 16 heads of 4 (3.9 TB/s), 6.6
+// TB/s with a row a key head (64 sequences of 16,384 keys, 8 heads).  Bound by those with more rows; latencies count, so eight warps
 // of one stage (four of three: half as fast), short chains, four keys' probabilities a load.
 #include "kvm_paged.cuh"
 #include "tc_primitives.cuh"

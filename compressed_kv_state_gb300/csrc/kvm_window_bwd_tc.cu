@@ -27,8 +27,10 @@
 // and under 113 KB of shared memory: two CTAs an SM, one's products beside the other's
 // rows.  A block's chain of product, rows, product is what bounds it (tensor pipe 28%
 // active, memory 24%), so the rows' part is kept short.  B4 H12 N8192 W512, the whole
-// backward: 437 us (rotation pass 46, dq 158, dk and dv 224, sinks 8); with the products
-// of a whole block at once 450; with one warpgroup of rows dk and dv alone took 255.
+// backward: 436 us (under a profiler: rotation pass 45, dq 160, dk and dv 234, sinks 6).  dk
+// and dv with the products of a whole block at once take 13 us more, with one warpgroup of
+// rows 31 more; without the wait of a half's products for the last readers of their place they
+// took 10 less.
 // All mbarrier waits are bounded; on expiry a CTA raises the status word, lets its copies
 // and MMAs land, and exits.
 #include <cuda.h>
@@ -579,8 +581,8 @@ __global__ void __launch_bounds__(NTHREADS, 2)
 }  // namespace kv
 
 // The sinks' rows from the parts, a CTA a row: a warp takes every JW-th part, two dims a lane,
-// and the warps are added up in their order (one warp a row: 689 us for the backward of B1
-// H16/4 N30011 W1024 where this takes 679).
+// and the warps are added up in their order (one warp a row: 10 us more for the backward of B1
+// H16/4 N30011 W1024, 691 us).
 constexpr int JW = 8;
 template <typename E>
 __global__ void __launch_bounds__(32 * JW) win_sink_kernel(Rows dk, Rows dv, const float* part, int parts, int S, int Hkv, int half,

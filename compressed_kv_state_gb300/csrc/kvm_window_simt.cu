@@ -11,10 +11,11 @@
 // dims) each: every product is 64 x 64 x 64 with two 16-byte shared loads per
 // 16 multiply-adds of a thread (two at once).  The next tiles come in by asynchronous
 // copies beside a tile's products.  Two CTAs an SM, so 128 registers (with the 148 that the
-// compiler takes otherwise one fits: 1,530 us for the backward below).  B2 H8/2 N4096 W512
-// S16 r32: forward 339 us (24.5 TFLOP/s; 372 without the copies ahead), backward 1,097
-// (18.9).  Bound by the latencies of shared loads and barriers: the multiply-add pipe is
-// 40% busy.  Sums are made in a fixed order.  fp32 layers run here: the tensor cores' own
+// compiler takes otherwise one fits: 1,530 us for the backward below), at which each kernel
+// spills a little (28, 24 and 52 bytes stored).  B2 H8/2 N4096 W512 S16 r32: forward 338 us
+// (24.5 TFLOP/s; 372 without the copies ahead), backward 1,092 (18.9).  No unit is near its
+// limit (the multiply-add pipe is 40% busy): what is left are the latencies of shared loads and
+// barriers.  Sums are made in a fixed order.  fp32 layers run here: the tensor cores' own
 // fp32 form keeps 10 bits of an operand.
 #include "kvm_window.cuh"
 

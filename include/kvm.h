@@ -390,8 +390,10 @@ typedef struct {
  * kvm_rope_table, at least n_tokens positions (ignored when rope_dims is 0).
  *   out_i = sum_j softmax_j(q'_i . k'_j / 8) v_j over the visible keys j,
  * q', k' the rotated q, k (for bf16 rounded to bf16, as the probabilities are;
- * sums and statistics are fp32).  A token no query sees through its mask never
- * reaches that query's output, whatever its values.  lse (optional): fp32
+ * sums and statistics are fp32).  A token that a query does not see never
+ * reaches its output, whatever its values; where a token that it sees has values
+ * that are not finite, the output's dims they reach are not either (infinite or
+ * NaN), and a query whose every score is -infinity gets NaN.  lse (optional): fp32
  * [B, H, n_tokens], the log2 of the sum of 2^(score * log2 e), for the
  * backward.  scratch: kvm_window_scratch_bytes(cfg, n_tokens, 0) bytes,
  * 256-byte aligned (0: invalid arguments).  n_tokens 0 does nothing. */
@@ -467,10 +469,11 @@ kvm_status kvm_paged_read(const kvm_paged_cache* cache, const kvm_rows* k, const
  * p = lens[b] - n_q + t (its key and value are in the cache already) and is
  * rotated there.  It sees the keys j <= p, and with window > 0 of these only
  * p - j < window or j < n_sinks (window 0: all, n_sinks ignored).  A query
- * that sees nothing (lens[b] < n_q) gets zeros.  lens[b] is held to
+ * that sees nothing (lens[b] < n_q), or nothing but scores of -infinity, gets zeros.  lens[b] is held to
  * [0, min(max_pages * page_size, rope_len)] and a visible key whose page index
  * is out of range is left out, both with KVM_DEV_DATA.  A key that a
- * query does not see never reaches its output, whatever its values.  Pages wholly behind
+ * query does not see never reaches its output, whatever its values; values that
+ * are not finite in one that it sees make the dims they reach so.  Pages wholly behind
  * the window and the sinks are not looked up.  scratch:
  * kvm_paged_attention_scratch_bytes bytes, 256-byte aligned. */
 size_t kvm_paged_attention_scratch_bytes(const kvm_paged_cache* cache, int32_t batch, int32_t heads,

@@ -145,8 +145,9 @@ def test_queries_before_the_first_token_beside_values_that_are_not_finite(dt, in
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
 @pytest.mark.parametrize("where", [0, 130, 5000])
 def test_a_value_that_later_queries_see_costs_the_window_nothing(dt, where):
-    """Under the causal mask a value that is not finite makes every later result so; the call takes
-    about its usual time (rows computed again key by key took 150 times that)."""
+    """Under the causal mask a value that is not finite makes every later result so; they are not
+    computed again key by key (which took 300 times the usual time).  At 5000 the eight rows of the
+    tile before it are, as they do not see it: 6 times; 20 leaves room for the clock."""
     from compressed_kv_state_gb300 import kvm
     g = torch.Generator().manual_seed(81)
     n = 16384 if dt == "bf16" else 6000
@@ -159,7 +160,7 @@ def test_a_value_that_later_queries_see_costs_the_window_nothing(dt, where):
         out = w.forward(q, k, v)
         assert not torch.isfinite(out[:, :, where:]).any()
         assert torch.equal(out[:, :, :where // 128 * 128 - 128], clean[:, :, :where // 128 * 128 - 128]) or where < 256
-        assert fastest(lambda: w.forward(q, k, v)) <= 10 * usual
+        assert fastest(lambda: w.forward(q, k, v)) <= 20 * usual
 
 
 # dtype, B, H, Hkv, N, W, S, r, layout
